@@ -582,6 +582,9 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_bwd_kernel(const NormBw
   const float inv_d = 1.f / (float)D;
   const int64_t m0 = id * p.rows, m1 = min(p.M, m0 + p.rows);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  // the other block's shared memory may be written once that block runs: the wait for it
+  // stands before the row loop (nothing else is ordered by it)
+  if constexpr (PAIR) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   grid_dependency_wait();
   grid_launch_dependents();
   RowRing<NT, VPT, FULL> rows{ring, nv, p.stages, m0, m1, p.D8};
@@ -621,6 +624,7 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_bwd_kernel(const NormBw
   int64_t gr = p.gate ? m0 / p.per : 0;                    // this row's gate row
   int64_t gend = p.gate ? min(m1, (gr + 1) * p.per) : m1;  // the first row past it, here
   bool first = true, fresh = true;
+  if constexpr (PAIR) asm volatile("barrier.cluster.wait;" ::: "memory");
   for (int64_t m = m0; m < m1; ++m) {
     const float rp = rp_next, rn = rn_next;
     if (m + 1 < m1) {
