@@ -410,9 +410,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       float sx = 0.f;
       if constexpr (C::kI8)
         if (row0 + lane < p.M) sx = __ldg(p.sx + row0 + lane);
-      if (!tc::mbar_wait(tfull_bar(b), (uint32_t)(i >> 1) & 1u, abort, err, 4096u)) break;
-      tc::fence_after();
+      // one answer for the warp: the reads below are of whole warps
       __syncwarp();
+      if (!tc::warp_wait(tfull_bar(b), (uint32_t)(i >> 1) & 1u, abort, err, 4096u)) break;
+      tc::fence_after();
       const uint32_t acc = tmem + (uint32_t)(b * BN) + ((uint32_t)(ew * 32) << 16);
       // 32 columns' data, broadcast to the lanes from shared memory
       auto column_data = [&](int n) {

@@ -44,3 +44,11 @@ def test_other_blocks_memory_is_touched_after_a_cluster_barrier(file, name, body
         return
     wait = re.search(r"barrier\.cluster\.wait|cluster_wait\(|cluster_sync\w*\(", body)
     assert wait is not None and wait.start() < access.start(), f"{name}: {access.group()} first"
+
+
+@pytest.mark.parametrize("name", ["pair_gemm_kernel", "thin_gemm_kernel"])
+def test_bounded_waits_answer_for_the_whole_warp(name):
+    """A wait that runs out may do so in some lanes of a warp only; warp-collective work
+    (tcgen05.ld, __syncwarp) may follow only an answer that its lanes share, warp_wait's."""
+    (body,) = [b for _, n, b in KERNELS if n == name]
+    assert "tc::warp_wait(" in body and "mbar_wait(" not in body
