@@ -454,6 +454,8 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormD
     if (threadIdx.x == 0) p.hs[m] = sc;
     const double by = rn * rcp_f64(sc);
     const bool live = sc > 0.f && sc < INFINITY;  // else (underflow, not a number) codes 0
+    // a subnormal scale is rounded coarsely: amax / scale may pass 127.5 there (up to 190)
+    const bool coarse = sc < 1.17549435e-38f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * B;
@@ -462,8 +464,9 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormD
         if (live) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint32_t q = (uint32_t)__double2loint(fma(t[k][j], by, 6755399441055744.0));
-            w[j >> 2] |= (q & 0xFFu) << (8 * (j & 3));
+            int q = __double2loint(fma(t[k][j], by, 6755399441055744.0));
+            if (coarse) q = max(-127, min(127, q));
+            w[j >> 2] |= ((uint32_t)q & 0xFFu) << (8 * (j & 3));
           }
         }
         p.hq[at + v] = make_uint2(w[0], w[1]);

@@ -5,7 +5,8 @@ from __future__ import annotations
 import pytest
 import torch
 
-from test_gpu_feedforward import _gen, _norm_inputs, _normal, _ok, test_residual_norm_backward as _check_backward
+from test_gpu_feedforward import (B, TINY, _gen, _norm64, _norm_inputs, _normal, _ok,
+                                  test_residual_norm_backward as _check_backward)
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +26,40 @@ def test_norm_backward_rows_shared_by_two_blocks(wq, M, D):
         again = wq.residual_norm_backward(dr, dh, x, y, gate, wp, wn, rp, rn)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
     _ok(wq)
+
+
+def _codes_are_the_definition(wq, x, y, gate, wp, wn, per, scale, eps=1e-6):
+    """Codes and scales equal those of 64 bits, clamped to +-127; returns them."""
+    r, q, s = wq.residual_norm(x, y, gate, wp, wn, rows_per_gate=per, scale=scale, eps=eps, quantize=True)
+    _ok(wq)
+    R, H, _, _ = _norm64(x, y, gate, per, wp, wn, scale, eps)
+    S = (H.abs().amax(1) / 127).float()
+    Q = torch.where(S[:, None] > 0, H / S.double()[:, None], torch.zeros_like(H)).round().clamp(-127, 127)
+    assert torch.equal(s, S), (s, S)
+    assert torch.equal(q, Q.to(torch.int8)), (q != Q).nonzero()[:4]
+    assert ((r.double() - R).abs() <= B * R.abs() + TINY).all()
+    return q, s
+
+
+@pytest.mark.parametrize("D", [8, 264, 2048, 4096])
+def test_codes_of_a_subnormal_scale(wq, D):
+    """A scale that is subnormal is rounded by up to a half: codes stop at +-127 in place of
+    changing their sign.  Rows enough for every form of the kernel."""
+    bf = torch.bfloat16
+    for M in (3, 700):
+        x = torch.full((M, D), 3.0, device="cuda", dtype=bf)
+        x[:, 0] = 0.05
+        wn = torch.zeros(D, device="cuda", dtype=bf)
+        wn[0] = 1e-40
+        q, s = _codes_are_the_definition(wq, x, None, None, None, wn, M, 1.0)
+        assert (s > 0).all() and (s < 2.0 ** -126).all()
+        # D = 8 (rms 2.81): amax / 127 is 9.2 x 2^-149, the scale 9, the quotient 129.9.  From
+        # D = 264 on (rms 2.99) amax / 127 is 8.6 x 2^-149, the scale 9 too, the code 122
+        assert D > 8 or (q[:, 0] == 127).all()
+        _codes_are_the_definition(wq, -x, None, None, None, wn, M, 1.0)
+        # tiny rows under an ordinary weight: from scales just above the normal range to none
+        zero = torch.zeros(M, D, device="cuda", dtype=bf)
+        y = (torch.linspace(0.2, 1.0, D, device="cuda") * 1e-30).to(bf).expand(M, D).contiguous()
+        one = torch.ones(D, device="cuda", dtype=bf)
+        for scale in (2e-9, 7e-10, 3e-12, 7e-15, 2.5e-16, 1.6e-16, 9e-17, 1e-17):
+            _codes_are_the_definition(wq, zero, y, None, None, one, M, scale)
