@@ -137,6 +137,39 @@ __device__ __forceinline__ double rcp_f64(float s) {
   return fma(fma(-d, y, 1.0), y, y);
 }
 
+// Whether each of eight bf16 values is zero or of a magnitude in [2^-E, 2^E], on the bit
+// patterns without their signs, two at a time: the least of (pattern - 1), where a zero
+// wraps to the top, and the largest pattern.  (An infinity or NaN is past every 2^E.)
+template <int E>
+__device__ __forceinline__ bool moderate(const uint4& v) {
+  constexpr unsigned lo = ((127 - E) << 7) - 1, hi = (127 + E) << 7;
+  const unsigned w[4] = {v.x, v.y, v.z, v.w};
+  unsigned least = 0xFFFFFFFFu, most = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned t = w[i] & 0x7FFF7FFFu;
+    least = __viaddmin_u16x2(t, 0xFFFFFFFFu, least);
+    most = __vmaxu2(most, t);
+  }
+  return __vminu2(least, lo << 16 | lo) == (lo << 16 | lo) &&
+         __vmaxu2(most, hi << 16 | hi) == (hi << 16 | hi);
+}
+
+// Four integers as bytes, each held to -128 .. 127.
+__device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
+  uint32_t hi, r;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(d), "r"(c), "r"(0));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(a), "r"(hi));
+  return r;
+}
+
+// (volatile: read again in every row, not kept in registers)
+__device__ __forceinline__ uint4 ld_again(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 struct NormDev {
   const uint4 *x, *y, *gate, *wpost, *wpre;
   int64_t M, D8, per;
@@ -340,10 +373,14 @@ __global__ void __launch_bounds__(MAXT, VPT == 4 ? 1 : 2) residual_norm_kernel(c
 // and the codes are the definition's.  What fp64 costs is conversions (F2F runs at an
 // eighth of fp32's rate): gate and w_post are joined in fp32, where their product is
 // exact, and so is its product with y (8 + 8 + 8 bits), so one conversion serves the
-// three.  r w_pre is kept: its largest magnitude gives the scale, found beside the sum
-// of squares with one barrier, and one fused multiply-add with 1.5 x 2^52 rounds
-// (r w_pre) (1 / (rms s)) to the nearest integer, half to even.  Bound by conversions
-// and issue slots: 8192 x 8192 164 us, 2.9 TB/s.
+// three.  That holds while no product leaves fp32's normal range: where a thread's gate and
+// w_post are in 2^-40 .. 2^40 and its y in 2^-46 .. 2^46, or zero; a thread with others
+// multiplies in fp64 (the test costs 2 to 6%; to redo the row, told by its maximum, cost 6
+// to 20%, by the registers that it held).  r w_pre is kept: its largest magnitude gives the
+// scale, found beside the sum of squares with one barrier, and one fused multiply-add with
+// 1.5 x 2^52 rounds (r w_pre) (1 / (rms s)) to the nearest integer, half to even.  w_pre is
+// read in every row, out of L1 (kept in registers it made others spill: 4096 x 4096 47 us,
+// so 41).  Bound by conversions and issue slots: 8192 x 8192 174 us, 2.7 TB/s.
 template <int VPT, int MAXT, bool FULL, bool EACH>
 __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormDev p) {
   constexpr int NT = EACH ? 3 : 2;
@@ -363,28 +400,30 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormD
   from[1] = p.y;
   if constexpr (EACH) from[2] = p.gate;
   rows.begin(from);
-  uint4 wn[VPT];
   F2 kk[VPT][4];  // gate w_post
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int v = threadIdx.x + k * B;
-    wn[k] = FULL || v < nv ? __ldg(p.wpre + v) : zero;
 #pragma unroll
     for (int j = 0; j < 4; ++j) kk[k][j] = f2(0.f);
   }
   int64_t gr = p.gate ? m0 / p.per : 0;
   int64_t gend = m0;
+  bool joined = true;  // this thread's gate and w_post may be joined in fp32
   for (int64_t m = m0; m < m1; ++m) {
     const uint4* st = rows.next(from);
     if (EACH || m == gend) {
       gend = p.gate ? (gr + 1) * p.per : m1;
+      joined = true;
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int v = threadIdx.x + k * B;
         if (FULL || v < nv) {
+          const uint4 gv = EACH ? st[(NT - 1) * nv + v] : p.gate ? __ldg(p.gate + gr * p.D8 + v) : bf16_ones();
+          const uint4 pv = p.wpost ? __ldg(p.wpost + v) : bf16_ones();
+          joined = joined && moderate<40>(gv) && moderate<40>(pv);
           F2 w[4];
-          unpack(EACH ? st[(NT - 1) * nv + v] : p.gate ? __ldg(p.gate + gr * p.D8 + v) : bf16_ones(), kk[k]);
-          unpack(p.wpost ? __ldg(p.wpost + v) : bf16_ones(), w);
+          unpack(gv, kk[k]);
+          unpack(pv, w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) kk[k][j] = kk[k][j] * w[j];
         }
@@ -412,22 +451,63 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormD
       if (threadIdx.x == 0 && p.rpost) p.rpost[m] = (float)rp;
       post *= rp;
     }
+    // y gate w_post
     double t[VPT][8];
+    bool plain = joined;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int v = threadIdx.x + k * B;
+      plain = plain && moderate<46>(p.y && (FULL || v < nv) ? st[nv + v] : zero);
+    }
+    if (plain) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int v = threadIdx.x + k * B;
+        F2 y[4];
+        unpack(p.y && (FULL || v < nv) ? st[nv + v] : zero, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 e = floats(y[j] * kk[k][j]);
+          t[k][2 * j] = (double)e.x;
+          t[k][2 * j + 1] = (double)e.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int v = threadIdx.x + k * B;
+        const bool in = FULL || v < nv;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[k][j] = 1.0;
+        auto times = [&](const uint4& by) {
+          F2 f[4];
+          unpack(by, f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 e = floats(f[j]);
+            t[k][2 * j] *= (double)e.x;
+            t[k][2 * j + 1] *= (double)e.y;
+          }
+        };
+        times(p.y && in ? st[nv + v] : zero);
+        if ((EACH || p.gate) && in) times(EACH ? st[(NT - 1) * nv + v] : __ldg(p.gate + (gr - 1) * p.D8 + v));
+        if (p.wpost && in) times(__ldg(p.wpost + v));
+      }
+    }
     double sum[1] = {0.0};
     unsigned long long top = 0;  // bits of the largest |r w_pre|
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * B;
-      F2 x[4], y[4], w[4];
+      F2 x[4], w[4];
       unpack(FULL || v < nv ? st[v] : zero, x);
-      unpack(p.y && (FULL || v < nv) ? st[nv + v] : zero, y);
-      unpack(wn[k], w);
+      unpack(FULL || v < nv ? ld_again(p.wpre + v) : zero, w);
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 xe = floats(x[j]), ye = floats(y[j] * kk[k][j]), we = floats(w[j]);
-        const double r0 = fma((double)ye.x, post, (double)xe.x);
-        const double r1 = fma((double)ye.y, post, (double)xe.y);
+        const float2 xe = floats(x[j]), we = floats(w[j]);
+        const double r0 = fma(t[k][2 * j], post, (double)xe.x);
+        const double r1 = fma(t[k][2 * j + 1], post, (double)xe.y);
         o[j] = pack_bf16((float)r0, (float)r1);
         sum[0] = fma(r0, r0, sum[0]);
         sum[0] = fma(r1, r1, sum[0]);
@@ -454,7 +534,8 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormD
     if (threadIdx.x == 0) p.hs[m] = sc;
     const double by = rn * rcp_f64(sc);
     const bool live = sc > 0.f && sc < INFINITY;  // else (underflow, not a number) codes 0
-    // a subnormal scale is rounded coarsely: amax / scale may pass 127.5 there (up to 190)
+    // a subnormal scale is rounded coarsely: amax / scale may pass 127.5 there (up to 190).
+    // The bytes are held to -128 .. 127 anyway, these to -127
     const bool coarse = sc < 1.17549435e-38f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -462,11 +543,14 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormD
       if (FULL || v < nv) {
         uint32_t w[2] = {0u, 0u};
         if (live) {
+          int q[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            int q = __double2loint(fma(t[k][j], by, 6755399441055744.0));
-            if (coarse) q = max(-127, min(127, q));
-            w[j >> 2] |= ((uint32_t)q & 0xFFu) << (8 * (j & 3));
+          for (int j = 0; j < 8; ++j) q[j] = __double2loint(fma(t[k][j], by, 6755399441055744.0));
+          w[0] = pack_s8(q[0], q[1], q[2], q[3]);
+          w[1] = pack_s8(q[4], q[5], q[6], q[7]);
+          if (coarse) {
+            w[0] = __vmaxs4(w[0], 0x81818181u);
+            w[1] = __vmaxs4(w[1], 0x81818181u);
           }
         }
         p.hq[at + v] = make_uint2(w[0], w[1]);

@@ -63,3 +63,42 @@ def test_codes_of_a_subnormal_scale(wq, D):
         one = torch.ones(D, device="cuda", dtype=bf)
         for scale in (2e-9, 7e-10, 3e-12, 7e-15, 2.5e-16, 1.6e-16, 9e-17, 1e-17):
             _codes_are_the_definition(wq, zero, y, None, None, one, M, scale)
+
+
+# magnitudes of y, gate and w_post whose product leaves fp32's normal range, or comes near its ends
+FAR = [(1e35, 100.0, 100.0), (1e35, 1e-36, 1e-20), (1e-35, 1e-10, 1.0), (1e-30, 1e-14, 1e-3), (1e30, 1e30, 1e-30),
+       (1e-39, 1e30, 1.0), (1e13, 1e12, 1e12), (1e-13, 1e-12, 1e-12), (1.0, 1e25, 1e-25), (1e-20, 1e-20, 1e20)]
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("D,M,per", [(8, 3, 1), (1032, 5, 2), (264, 700, 1), (4096, 700, 64), (2048, 400, 1)])
+def test_codes_where_gate_and_norm_leave_fp32(wq, D, M, per, post):
+    """Codes are the definition's whatever the magnitudes of y, gate and w_post; rows whose r is
+    the far product alone among them, zeros and ordinary columns beside far ones."""
+    g = _gen(D + M)
+    for big, gt, wt in FAR:
+        x, y, gate, wp, wn = _norm_inputs(g, M, D, per)
+        x[::2] = 0
+        y, gate, wp = (y.float() * big).bfloat16(), (gate.float() * gt).bfloat16(), (wp.float() * wt).bfloat16()
+        y[:, 3::16] = 0
+        y[:, 5::32] = 1.0
+        gate[:, 6::16] = 0
+        gate[:, 1::32] = -0.5
+        R, _, _, _ = _norm64(x, y, gate, per, wp if post else None, wn, 0.7, 1e-30)
+        if not (R.abs() < 3e38).all():  # r itself is no number of its type
+            continue
+        _codes_are_the_definition(wq, x, y, gate, wp if post else None, wn, per, 0.7, eps=1e-30)
+
+
+def test_codes_and_bf16_agree_on_a_far_row(wq):
+    """y near 1e35 with gate and w_post near 100: r and h are ordinary numbers in both forms."""
+    g = _gen(5)
+    x, y, gate, wp, wn = _norm_inputs(g, 6, 512, 3)
+    y, gate, wp = (y.float() * 1e35).bfloat16(), (gate.float() * 100).bfloat16(), (wp.float() * 100).bfloat16()
+    r, h = wq.residual_norm(x, y, gate, wp, wn, rows_per_gate=3)
+    r2, q, s = wq.residual_norm(x, y, gate, wp, wn, rows_per_gate=3, quantize=True)
+    _ok(wq)
+    assert torch.isfinite(h).all() and torch.isfinite(s).all()
+    # bf16 of both, and half a step of the codes
+    assert ((q.double() * s.double()[:, None] - h.double()).abs() <= 0.51 * s.double()[:, None] + 2 * B * h.double().abs()).all()
+    assert ((r.double() - r2.double()).abs() <= 2 * B * r.double().abs()).all()
