@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_bwd_kernel(const NormBw
       unpack(in ? st[v] : zero, f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        ky[j] = ky[j] * (kk[k][j] * f2(rp));  // k yhat
+        ky[j] = ky[j] * f2(rp) * kk[k][j];  // k yhat (k / rms(y) may leave fp32)
         rh[k][j] = (f[j] + ky[j]) * f2(rn);
       }
       unpack(in && p.dr ? st[2 * nv + v] : zero, t[k]);

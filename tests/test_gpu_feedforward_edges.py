@@ -5,7 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
-from test_gpu_feedforward import (B, TINY, _gen, _norm64, _norm_inputs, _normal, _ok,
+from test_gpu_feedforward import (B, TINY, _gen, _norm64, _norm_inputs, _normal, _ok, _within,
                                   test_residual_norm_backward as _check_backward)
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +102,39 @@ def test_codes_and_bf16_agree_on_a_far_row(wq):
     # bf16 of both, and half a step of the codes
     assert ((q.double() * s.double()[:, None] - h.double()).abs() <= 0.51 * s.double()[:, None] + 2 * B * h.double().abs()).all()
     assert ((r.double() - r2.double()).abs() <= 2 * B * r.double().abs()).all()
+
+
+@pytest.mark.parametrize("per", [1, 3])
+@pytest.mark.parametrize("D", [264, 8200])
+def test_norm_backward_of_far_y_and_small_gates(wq, D, per):
+    """y near bf16's largest numbers under small gates: yhat is ordinary, and so is r / rms(r)
+    where r is the gated norm alone.  (1 / rms(y) may be subnormal in fp32: 2^-21 relative.)"""
+    M, scale, eps = 7, 0.7, 1e-30
+    g = _gen(D + per)
+    x, y, gate, wp, wn = _norm_inputs(g, M, D, per)
+    x[::2] = 0
+    y, gate = (y.float().clamp(-1.5, 1.5) * 2e38).bfloat16(), (gate.float() * 1e-7).bfloat16()
+    dr, dh = _normal(g, M, D), _normal(g, M, D)
+    _, _, rp, rn = wq.residual_norm(x, y, gate, wp, wn, rows_per_gate=per, scale=scale, eps=eps, save=True)
+    dx, _, dgate, dwp, dwn = wq.residual_norm_backward(dr, dh, x, y, gate, wp, wn, rp, rn, rows_per_gate=per,
+                                                       scale=scale)
+    _ok(wq)
+    rows = torch.arange(M, device="cuda") // per
+    Y, G = y.double(), gate.double()[rows]
+    RP = (Y.square().mean(1, keepdim=True) + eps).rsqrt()
+    yh = Y * RP
+    R = x.double() + scale * G * yh * wp.double()
+    RN = (R.square().mean(1, keepdim=True) + eps).rsqrt()
+    rh, a = R * RN, dh.double() * wn.double()
+    ref = dr.double() + RN * (a - rh * (a * rh).mean(1, keepdim=True))
+    size = dr.double().abs() + RN * (a.abs() + rh.abs() * (a * rh).abs().mean(1, keepdim=True))
+    small = 2.0 ** -17
+    _within(dx, ref, B * ref.abs() + small * size, "dx")
+    t, s = dh.double() * rh, (dh.double() * rh).abs()
+    _within(dwn, t.sum(0), B * t.sum(0).abs() + small * s.sum(0), "dw_pre")
+    t, s = scale * ref * G * yh, scale * size * (G * yh).abs()
+    _within(dwp, t.sum(0), B * t.sum(0).abs() + small * s.sum(0), "dw_post")
+    t, s = scale * ref * yh * wp.double(), scale * size * (yh * wp.double()).abs()
+    zero = torch.zeros(gate.shape, device="cuda", dtype=torch.float64)
+    want = zero.index_add(0, rows, t)
+    _within(dgate, want, B * want.abs() + small * zero.index_add(0, rows, s), "dgate")
