@@ -15,7 +15,8 @@ shapes or devices raise ``ValueError`` before anything is launched, what the
 library refuses raises ``WQError``.
 
 ``gated_ff`` and ``residual_norm`` are differentiable where an input requires a gradient
-(once, and not inside CUDA graph capture).  With ``save=True`` they return what the explicit
+(once, not inside CUDA graph capture, and in reverse mode only: a tensor that carries a
+forward-mode tangent is refused).  With ``save=True`` they return what the explicit
 ``..._backward`` calls take and are not recorded by autograd; these forward and backward
 calls may be captured into CUDA graphs.
 """
@@ -25,6 +26,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 from . import ACTIVATIONS, WQ_OK, _lib, _check
 
@@ -37,6 +39,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _dual_level():
+    # the level of torch.autograd.forward_ad that is entered (-1: none)
+    return getattr(forward_ad, "_current_level", 0)
+
+
+def _no_tangents(where, ts):
+    # the kernels see the primal alone: its derivative would read as zero
+    for t in ts:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{where} has no forward-mode derivative: a tensor carries a tangent")
+
+
 def _placed(fn):
     """Runs ``fn(first tensor, ...)`` with the tensor's device and the wanted stream current."""
     @functools.wraps(fn)
@@ -45,6 +59,8 @@ def _placed(fn):
             (a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{fn.__name__}: CUDA tensors are needed (there is no CPU form)")
+        if _dual_level() >= 0:
+            _no_tangents(fn.__name__, (*args, *kw.values()))
         if stream is None and t.get_device() == _device():
             return fn(*args, **kw)
         if stream is None:
