@@ -59,3 +59,21 @@ def test_forward_mode_is_refused(wq):
         assert torch.equal(wq.gated_ff(forward_ad.unpack_dual(d).primal, x, x), want)
     torch.cuda.synchronize()
     assert wq.wq_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_quantize_rows_int8_of_a_recorded_tensor(wq):
+    """Codes and scales have no gradient: an input that requires one is refused unless the
+    caller says that none is wanted."""
+    x = torch.ones(4, 64, device="cuda", dtype=torch.bfloat16)
+    want = wq.quantize_rows_int8(x)
+    p = x.clone().requires_grad_(True)
+    with pytest.raises(ValueError, match="detach"):
+        wq.quantize_rows_int8(p)
+    with pytest.raises(ValueError, match="detach"):
+        wq.quantize_rows_int8(p * 2)
+    taken = [wq.quantize_rows_int8(p.detach())]
+    with torch.no_grad():
+        taken.append(wq.quantize_rows_int8(p))
+    for got in taken:
+        assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
