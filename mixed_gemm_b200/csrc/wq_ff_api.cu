@@ -1,7 +1,6 @@
 // C ABI of the feed-forward operators (include/wq.h): argument checks and
 // dispatch.  Every check runs on the host before anything is launched.
 #include <math.h>
-#include <stdlib.h>
 
 #include "wq_act_fn.cuh"
 #include "wq_ff.cuh"
@@ -47,16 +46,18 @@ int status(cudaError_t e) {
 // the weight once into registers and reads all tokens once per 16 weight rows; THIN
 // (at most 128 tokens) runs tcgen05 with the weight as the 128-row operand; PAIR with the
 // tokens as rows of 256 x 256 tiles.  Measured (weights past L2), us, FEW / THIN / PAIR:
-//   INT8 2048 x 2048     8 tokens 2.1 / 4.0 / 6.3    32: 3.0 / 4.1 / 7.1   128: - / 6.4 / 5.9
-//   INT8 4096 x 4096    16 tokens 5.6 / 6.8 / 13     32: 7.2 / 7.0 / 9.5   128: - / 9.8 / 9.8
-//   INT8 8192 x 8192     8 tokens 14.3 / 13.8 / 27   32: 21.8 / 14.2 / 19  128: - / 16.9 / 19.7
-//   INT8 28672 x 8192    8 tokens 40.4 / 39.2 / 62   32: 69.6 / 39.8 / 54  128: - / 44.2 / 56.5
-//   gated 28672 x 8192   8 tokens 143 / 139 / 190    32: 254 / 141 / 193   128: - / 157 / 200
+//                        8 tokens             16                   32                  128
+//   INT8 2048 x 2048      2.8 / 5.2 / 7.5      3.0 / 5.0 / 6.7      3.9 / 4.9 / 6.7     - / 6.4 / 5.9
+//   INT8 4096 x 4096      5.1 / 7.2 / 13.6     5.7 / 7.1 / 13.7     7.5 / 7.4 / 9.6     - / 9.8 / 9.8
+//   INT8 8192 x 8192     13.6 / 14.7 / 27.0   15.4 / 15.0 / 18.0   22.0 / 15.2 / 18.4   - / 16.9 / 19.7
+//   INT8 28672 x 8192    40.2 / 39.7 / 57.6   50.0 / 39.6 / 49.6   69.5 / 40.0 / 50.0   - / 44.2 / 56.5
+//   gated 4096 x 4096    13.6 / 15.6 / 30.3   16.4 / 15.8 / 19.9   21.3 / 16.2 / 20.0
+//   gated 28672 x 8192    143 / 141 / 190      163 / 142 / 191      233 / 142 / 192     - / 157 / 200
+// (one token: 13.1 / 14.5 and 38.4 / 41.2 for the larger two INT8 ones.)  Deep layers of few
+// rows are the exception: 500 x 16384 takes 7.5 / 7.1 with 8 tokens, 10 / 7.2 with 16 and
+// 16 / 7.3 with 32, where THIN splits k.
 enum Path { FEW, THIN, PAIR };
 Path path_for(int64_t M, int64_t rows) {
-#ifdef WQ_TUNING
-  if (const char* v = getenv("WQ_FF_PATH")) return v[0] == 'f' ? FEW : v[0] == 't' ? THIN : PAIR;
-#endif
   if (M <= 8 || (M <= 16 && rows <= 6144) || (M <= 32 && rows <= 2048)) return FEW;
   return M <= 128 ? THIN : PAIR;
 }
