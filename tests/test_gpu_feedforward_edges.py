@@ -138,3 +138,31 @@ def test_norm_backward_of_far_y_and_small_gates(wq, D, per):
     zero = torch.zeros(gate.shape, device="cuda", dtype=torch.float64)
     want = zero.index_add(0, rows, t)
     _within(dgate, want, B * want.abs() + small * zero.index_add(0, rows, s), "dgate")
+
+
+def test_i8_extreme_codes_longest_k_many_tokens(wq):
+    """-128 x -128 over the longest K with more tokens than the narrow kernels take; exact in fp32
+    (2^14 K and -127 x 2^7 K are K times whole numbers below 2^15, K = 2^17 - 16)."""
+    M, N, K = 200, 48, 131056
+    xq = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    xq[3::7] = 127
+    w = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    w[1::2] = 127
+    one = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    y = wq.matmul_i8(xq, one[0], w, one[1], out_dtype=torch.float32)
+    _ok(wq)
+    assert torch.equal(y, ((xq[:, :1].double() * K) * w[:, 0].double()).float())
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_i8_nan_scale_stays_in_its_row_of_many(wq, out_dtype):
+    g = _gen(6)
+    M, N, K = 200, 80, 64
+    xq = torch.randint(-128, 128, (M, K), device="cuda", generator=g).to(torch.int8)
+    w = torch.randint(-128, 128, (N, K), device="cuda", generator=g).to(torch.int8)
+    sx, sw = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    sx[2], sw[5] = float("nan"), float("nan")
+    y = wq.matmul_i8(xq, sx, w, sw, out_dtype=out_dtype)
+    _ok(wq)
+    rows, cols = torch.arange(M, device="cuda") != 2, torch.arange(N, device="cuda") != 5
+    assert torch.isnan(y[2]).all() and torch.isnan(y[:, 5]).all() and torch.isfinite(y[rows][:, cols]).all()
