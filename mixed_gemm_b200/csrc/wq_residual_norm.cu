@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(MAXT, VPT == 4 ? 1 : 2) residual_norm_kernel(c
 // scale, found beside the sum of squares with one barrier, and one fused multiply-add with
 // 1.5 x 2^52 rounds (r w_pre) (1 / (rms s)) to the nearest integer, half to even.  w_pre is
 // read in every row, out of L1 (kept in registers it made others spill: 4096 x 4096 47 us,
-// so 41).  Bound by conversions and issue slots: 8192 x 8192 174 us, 2.7 TB/s.
+// so 41).  Bound by conversions and issue slots: 8192 x 8192 153 us, 3.1 TB/s.
 template <int VPT, int MAXT, bool FULL, bool EACH>
 __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormDev p) {
   constexpr int NT = EACH ? 3 : 2;
@@ -607,9 +607,10 @@ cudaError_t launch_norm(const NormDev& p, cudaStream_t st) {
   const bool few = p.M <= sms, some = p.M <= 4 * sms;
   if (p.hq) {
     if (nv <= 1024 && (few || nv < 64)) return launch_rows<1, true, EACH>(p, 1024, st);
-    // (8140 x 4096: 84 us with two, 79 with four; 8192 x 8192 164, 166; 10000 x 2560,
-    // where four leave lanes idle, 71, 84)
-    if (nv >= 256 && nv <= 512 && nv % 128 == 0 && !some)
+    // four where they fill the lanes of every warp.  us with two / four: 8140 x 2048 46.3 /
+    // 40.6, 4096 88.5 / 74.6 (a gate row a token 90.2 / 83.9), 6144 141 / 130, 8192 174 / 153,
+    // 39000 x 1024 98.6 / 81.9; 10240 124 / 126; lanes idle in 2560 109 / 125, 4608 115 / 121
+    if (nv >= 128 && nv <= 1024 && nv % 128 == 0 && !some)
       return launch_rows<4, true, EACH>(p, 512, st);
     return launch_rows<2, true, EACH>(p, 1024, st);
   }
