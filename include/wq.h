@@ -389,7 +389,8 @@ int wq_gated_ff(const void* x, const void* w_gate, const void* w_up, const void*
  *   dw_gate, dw_up   device bf16 [F, K], both or neither
  *   db_gate, db_up   device bf16 [F], both or neither
  * Sums are fp32 and ordered (the same inputs give the same bits); the bias sums
- * take the unrounded dg, du.  With M == 0 the weight and bias gradients are
+ * take the unrounded dg, du.  The two roundings of dx and dW (dg or du, and the
+ * output) leave them 2.3e-3 off in the root mean square, where one leaves 1.7e-3.  With M == 0 the weight and bias gradients are
  * zeros.  Shapes and overlap rules as wq_gated_ff.  Asynchronous. */
 int wq_gated_ff_backward_workspace_size(int64_t M, int64_t F, int64_t K, int need_bias,
                                         size_t* bytes);
@@ -412,8 +413,10 @@ int wq_gated_ff_backward(const void* dh, const void* x, const void* w_gate, cons
  *   hq, hs     device int8 [M, D] and f32 [M], both or neither: h quantized per
  *              token as wq_quantize_act_int8 does (hs = fp32(amax / 127), codes
  *              round half to even of h / hs), but from the unrounded h; the input
- *              of wq_matmul_i8.  With them everything up to the codes is fp64.
- *              A row with a NaN or an infinity gets scale NaN and codes 0.
+ *              of wq_matmul_i8.  With them everything up to the codes is fp64,
+ *              whatever the magnitudes of y, gate and w_post (codes stop at +-127
+ *              where hs is subnormal and so rounded coarsely); without them r and
+ *              h are fp32 up to their one rounding.  A row with a NaN or an infinity gets scale NaN and codes 0.
  *   rstd_post, rstd_pre  device f32 [M] or NULL: kept for the backward pass
  * w_pre goes with h and / or hq, hs (at least one of them; none without w_pre).
  * h is taken from the unrounded r.  D % 8 == 0, D <= 16384; eps >= 1e-30.  M == 0 is a

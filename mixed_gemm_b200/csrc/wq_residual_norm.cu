@@ -233,7 +233,7 @@ struct RowRing {
 
 // A block takes consecutive rows, VPT 16-byte vectors of each a thread, with the rows
 // ahead on their way (one row per block with plain loads left the memory idle during the
-// two row sums: 8192 x 8192 took 113 us, this one 102, 5.2 TB/s: two barriers a row with
+// two row sums: 8192 x 8192 took 113 us, this one 104, 5.2 TB/s: two barriers a row with
 // 16 warps an SM).  scale gate w_post and w_pre stay in registers.
 //
 // Sums of squares are fp32, per thread and then over the block.  Squares of values past
@@ -375,12 +375,13 @@ __global__ void __launch_bounds__(MAXT, VPT == 4 ? 1 : 2) residual_norm_kernel(c
 // exact, and so is its product with y (8 + 8 + 8 bits), so one conversion serves the
 // three.  That holds while no product leaves fp32's normal range: where a thread's gate and
 // w_post are in 2^-40 .. 2^40 and its y in 2^-46 .. 2^46, or zero; a thread with others
-// multiplies in fp64 (the test costs 2 to 6%; to redo the row, told by its maximum, cost 6
-// to 20%, by the registers that it held).  r w_pre is kept: its largest magnitude gives the
+// multiplies in fp64 (the test costs 2 to 6%; to redo the row, told by its maximum, cost 11
+// to 28%, by the registers that it held).  r w_pre is kept: its largest magnitude gives the
 // scale, found beside the sum of squares with one barrier, and one fused multiply-add with
 // 1.5 x 2^52 rounds (r w_pre) (1 / (rms s)) to the nearest integer, half to even.  w_pre is
 // read in every row, out of L1 (kept in registers it made others spill: 4096 x 4096 47 us,
-// so 41).  Bound by conversions and issue slots: 8192 x 8192 153 us, 3.1 TB/s.
+// so 41).  8192 x 8192 153 us, 3.1 TB/s: conversions and issue slots are at 51% each, with
+// 16 warps an SM to hide a row's chain of sums behind.
 template <int VPT, int MAXT, bool FULL, bool EACH>
 __global__ void __launch_bounds__(MAXT, 1) residual_norm_int8_kernel(const NormDev p) {
   constexpr int NT = EACH ? 3 : 2;
@@ -636,7 +637,8 @@ cudaError_t launch_norm(const NormDev& p, cudaStream_t st) {
 // ahead into shared memory (cp.async, only the thread itself reads them, so no
 // barrier), and keeps the column sums.  Blocks' sums leave as one partial row each,
 // added in block order by a second kernel: results do not depend on timing.  8140 x
-// 4096 76 to 83 us, 5.2 to 4.8 TB/s; issue slots are 60% full.
+// 4096 82 to 85 us, 4.9 to 4.7 TB/s.  Neither DRAM (52 to 55%) nor the issue slots (50%)
+// are full: what bounds it is latency, with one 512-thread block an SM.
 struct NormBwdDev {
   const uint4 *dr, *dh, *x, *y, *gate, *wpost, *wpre;
   const float *rpost, *rpre;

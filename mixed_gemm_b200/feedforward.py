@@ -235,7 +235,10 @@ def gated_ff_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,
                       w_up: torch.Tensor, g: torch.Tensor, u: torch.Tensor, act: str = "silu",
                       need_dx: bool = True, need_dw: bool = True, need_bias: bool = False):
     """Gradients of ``gated_ff`` from dh = dL/dh [..., F] and the kept g, u: (dx, dw_gate, dw_up,
-    db_gate, db_up), None for what is not asked for."""
+    db_gate, db_up), None for what is not asked for.
+
+    dg and du are rounded to bf16, the operands of the products that make dx and the weights'
+    gradients; the bias gradients are sums of the unrounded ones."""
     f = "gated_ff_backward"
     xr = _rows(f, "x", x, _BF16)
     M, K = xr.shape
