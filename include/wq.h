@@ -297,7 +297,8 @@ int wq_linear_a8(const void* x, const void* packed_w, const void* scales, const 
                  size_t workspace_bytes, void* out, void* stream);
 
 /* The per-token INT8 activation quantizer of wq_linear_a8 on its own (device
- * buffers): xq int8 [M, K] (16-byte aligned), sx f32 [M]; K % 8 == 0.
+ * buffers): xq int8 [M, K] (16-byte aligned), sx f32 [M]; K % 8 == 0.  A row
+ * with a NaN or an infinity gets scale NaN and codes 0.
  * Source: as wq_linear_a8. */
 int wq_quantize_act_int8(const void* x, int64_t M, int64_t K, void* xq, void* sx, void* stream);
 

@@ -7,7 +7,8 @@
 //
 // The quotient amax / 127 is taken in fp64 and rounded once to fp32, and each
 // x / s_x in fp64 (IEEE division) before the rounding to an integer, so the
-// codes are the ones this definition gives, decision for decision.  One
+// codes are the ones this definition gives, decision for decision.  A row with a NaN or an
+// infinity has no such scale: it gets scale NaN and codes 0.  One
 // thread block per token row: a maximum pass, then a quantize pass, both
 // with 16-byte loads of eight bf16 values.
 #include "wq_internal.cuh"
@@ -19,28 +20,26 @@ namespace {
 __global__ void __launch_bounds__(256) quant_act_int8_kernel(const uint4* __restrict__ x,
                                                             int64_t K8, uint2* __restrict__ xq,
                                                             float* __restrict__ sx) {
-  __shared__ float red[8];
+  __shared__ unsigned red[8];
   __shared__ float s_row;
   const int64_t m = blockIdx.x;
   const uint4* row = x + m * K8;
-  float amax = 0.f;
+  unsigned top = 0;  // bits of the largest magnitude (they order as the values do, NaN on top)
   for (int64_t i = threadIdx.x; i < K8; i += blockDim.x) {
     const uint4 v = __ldg(row + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      amax = fmaxf(amax, fabsf(__uint_as_float(w[j] << 16)));
-      amax = fmaxf(amax, fabsf(__uint_as_float(w[j] & 0xFFFF0000u)));
+      top = max(top, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float a = 0.f;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) a = fmaxf(a, red[i]);
-    const float s = __double2float_rn((double)a / 127.0);
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) top = max(top, red[i]);
+    const float a = __uint_as_float(top);
+    const float s = top < 0x7F800000u ? __double2float_rn((double)a / 127.0) : __uint_as_float(0x7FC00000u);
     s_row = s;
     sx[m] = s;
   }
@@ -55,7 +54,7 @@ __global__ void __launch_bounds__(256) quant_act_int8_kernel(const uint4* __rest
     for (int j = 0; j < 8; ++j) {
       const uint32_t h = (j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16);
       int q = 0;
-      if (s != 0.f) {
+      if (s > 0.f) {
         q = __double2int_rn((double)__uint_as_float(h) / sd);
         q = q > 127 ? 127 : (q < -127 ? -127 : q);
       }

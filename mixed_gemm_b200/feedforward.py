@@ -151,7 +151,8 @@ def _size(where, *args):
 def quantize_rows_int8(x: torch.Tensor):
     """bf16 [..., K] -> (int8 codes [..., K], fp32 scales [...]): scale = max |x| / 127 of each
     row, codes round half to even (K % 8 == 0).  For activations (a scale per token) and for
-    the weight of ``matmul_i8`` (a scale per output channel).  Neither has a gradient."""
+    the weight of ``matmul_i8`` (a scale per output channel).  A row with a NaN or an infinity
+    gets scale NaN and codes 0.  Neither output has a gradient."""
     if _needs_grad(x):
         raise ValueError("quantize_rows_int8 has no backward pass: detach x")
     rows = _rows("quantize_rows_int8", "x", x, _BF16)

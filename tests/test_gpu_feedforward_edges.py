@@ -166,3 +166,28 @@ def test_i8_nan_scale_stays_in_its_row_of_many(wq, out_dtype):
     _ok(wq)
     rows, cols = torch.arange(M, device="cuda") != 2, torch.arange(N, device="cuda") != 5
     assert torch.isnan(y[2]).all() and torch.isnan(y[:, 5]).all() and torch.isfinite(y[rows][:, cols]).all()
+
+
+@pytest.mark.parametrize("K", [8, 64, 4104])
+@pytest.mark.parametrize("bad", [float("nan"), -float("nan"), float("inf"), -float("inf")])
+def test_quantize_rows_of_non_finite_values(wq, K, bad):
+    """A row with a NaN or an infinity has no scale: NaN, and codes 0 (as the norms' codes); the
+    product then shows it.  The other rows are the definition's, bf16's largest values among them."""
+    g = _gen(K)
+    x = _normal(g, 6, K)
+    x[1, K - 1] = x[4, 0] = bad
+    x[5] = torch.finfo(torch.bfloat16).max
+    x[2] = 0
+    q, s = wq.quantize_rows_int8(x)
+    _ok(wq)
+    good = torch.tensor([0, 2, 3, 5], device="cuda")
+    assert torch.isnan(s[[1, 4]]).all() and not q[[1, 4]].any()
+    X = x[good].double()
+    S = (X.abs().amax(1) / 127).float()
+    Q = torch.where(S[:, None] > 0, X / S.double()[:, None], torch.zeros_like(X)).round().clamp(-127, 127)
+    assert torch.equal(s[good], S) and torch.equal(q[good], Q.to(torch.int8))
+    if K % 16 == 0:
+        w, sw = wq.quantize_rows_int8(_normal(g, 24, K))
+        y = wq.matmul_i8(q, s, w, sw, out_dtype=torch.float32)
+        _ok(wq)
+        assert torch.isnan(y[[1, 4]]).all() and not torch.isnan(y[good]).any()
