@@ -391,8 +391,8 @@ int wq_gated_ff(const void* x, const void* w_gate, const void* w_up, const void*
  *   db_gate, db_up   device bf16 [F], both or neither
  * Sums are fp32 and ordered (the same inputs give the same bits); the bias sums
  * take the unrounded dg, du.  The two roundings of dx and dW (dg or du, and the
- * output) leave them 2.3e-3 off in the root mean square, where one leaves 1.7e-3.  With M == 0 the weight and bias gradients are
- * zeros.  Shapes and overlap rules as wq_gated_ff.  Asynchronous. */
+ * output) leave them 2.3e-3 off in the root mean square, where one leaves 1.7e-3.
+ * With M == 0 the weight and bias gradients are zeros.  Shapes and overlap rules as wq_gated_ff.  Asynchronous. */
 int wq_gated_ff_backward_workspace_size(int64_t M, int64_t F, int64_t K, int need_bias,
                                         size_t* bytes);
 int wq_gated_ff_backward(const void* dh, const void* x, const void* w_gate, const void* w_up,

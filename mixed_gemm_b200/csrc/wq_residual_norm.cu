@@ -637,7 +637,7 @@ cudaError_t launch_norm(const NormDev& p, cudaStream_t st) {
 // ahead into shared memory (cp.async, only the thread itself reads them, so no
 // barrier), and keeps the column sums.  Blocks' sums leave as one partial row each,
 // added in block order by a second kernel: results do not depend on timing.  8140 x
-// 4096 82 to 85 us, 4.9 to 4.7 TB/s.  Neither DRAM (52 to 55%) nor the issue slots (50%)
+// 4096 83 to 86 us, 4.8 to 4.7 TB/s.  Neither DRAM (52 to 55%) nor the issue slots (50%)
 // are full: what bounds it is latency, with one 512-thread block an SM.
 struct NormBwdDev {
   const uint4 *dr, *dh, *x, *y, *gate, *wpost, *wpre;
